@@ -327,6 +327,11 @@ int pa_decode_reserve(pa_pool *pool, int max_seqs, int max_q_heads);
  * out is aligned to its elements (else PA_ERR_INVALID_ARG); 16-token blocks of
  * 128-wide heads and a 16-byte-aligned out take the tcgen05 kernel, every other
  * call a plain one.
+ * Arithmetic of the tcgen05 kernel: queries on code pools keep 2^-12 of each
+ * element, or 2^-25 of the row's largest.  A weight is off by at most 2^-12 (bf16
+ * out; bf16 pools 2^-16) or 2^-20 (fp32 out) of itself, and on code pools by
+ * 2^-38 (bf16 out) or 2^-32 (fp32 out) of the largest weight, a weight being the
+ * key's times its block's value scale.
  * Workspace: partials of split contexts, grown on demand (cudaMalloc);
  * pa_decode_window_reserve sizes it ahead of time, for any window (for a
  * PA_FP8E4M3_BLOCK pool, pa_decode_reserve does).  Calls on one pool must not

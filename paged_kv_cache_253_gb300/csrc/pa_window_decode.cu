@@ -8,14 +8,24 @@
 //   O^T[128 dims x N]  += V^T[128 x 128] . P^T
 // and nothing is done to a key or value after its copy into shared memory.
 // Code pools feed the e4m3 codes to the tensor cores as they are
-// (kind::f8f6f4), which wants e4m3 on the N side too: a query is the sum of
-// three e4m3 parts, each the remainder of the last one times 16, and so are the
-// weights (three parts for a bf16 result, five for fp32).  The parts are extra
-// columns, which are free: the MMAs' time goes by the M side's reads of shared
-// memory.  Error of n parts: 2^-4n of the number, or 2^(-6-4n) of the unit;
+// (kind::f8f6f4), which wants 8 bits on the N side too: a query is the sum of
+// three e4m3 parts, each the remainder of the last one times 16.  The parts are
+// extra columns, which are free: the MMAs' time goes by the M side's reads of
+// shared memory.  Error of n parts: 2^-4n of the number, or 2^(-6-4n) of the unit;
 // queries are first scaled by a power of two that puts the row's largest
-// element into [2^7, 2^8), weights so that the largest is 2^4 .. 2^8.  bf16
-// pools take the weights as two or three bf16 parts.
+// element into [2^7, 2^8).
+// Weights span more binary orders than a query's elements: many small ones
+// together may count as much as the largest, or be all of the result where the
+// largest one's value is zero, so the smallest part's last place matters, not
+// only the largest weight's error.  For a bf16 result they are four e5m2 parts,
+// each the remainder of the last one times 8 (error 2^-12 of the weight, or 2^-26
+// of the unit), with the largest at 2^12 .. 2^15: what is cut off is under 2^-38
+// of the largest weight per key.  (Three e4m3 parts with the largest at 2^4 ..
+// 2^8, 2^-22, lost half of 131072 weights of e^-15.5.)  For fp32 they are five e4m3
+// parts (2^-20 of the weight, or 2^-26 of the unit), the largest at 2^6 .. 2^8.5:
+// 2^-32 of the largest per key.  (2^7 .. 2^8.5 raises references more often: 256
+// sequences on a window, 147 -> 156 us.)  bf16 pools take the weights as two or three
+// bf16 parts, which have a float's range.
 //
 // A block's key scale multiplies its tokens' scores.  Its value scale goes into
 // the weights, w = 2^(x + log2 ev - r_o), with a reference r_o of their own (a
@@ -110,7 +120,13 @@ struct Misc {
 template <bool CODE, bool WIDE, int GM>      // WIDE: fp32 output
 struct Cfg {
     static constexpr int kQParts = CODE ? 3 : 1;
-    static constexpr int kPParts = CODE ? (WIDE ? 5 : 3) : (WIDE ? 3 : 2);
+    static constexpr int kPParts = CODE ? (WIDE ? 5 : 4) : (WIDE ? 3 : 2);
+    // code pools' weights (see above): the factor between two parts; the largest weight
+    // is 2^kLift when a reference is set, 2^(kLift + kLag) when it is raised (e5m2 holds
+    // up to 2^15.8, e4m3 up to 2^8.8)
+    static constexpr bool kE5 = CODE && !WIDE;
+    static constexpr float kPart = kE5 ? 8.f : 16.f;
+    static constexpr float kLift = !CODE ? 0.f : WIDE ? 6.f : 12.f, kLag = !CODE ? 8.f : WIDE ? 2.5f : 3.f;
     // The tensor cores cut a sum to fp32 after each 16 keys, always towards zero: over
     // 30000 bf16 keys that made a result 1e-5 smaller than it is.  For fp32 outputs each
     // step's product starts from zero and the steps are added in registers, rounded to
@@ -173,15 +189,23 @@ __device__ __forceinline__ uint64_t plain_desc(uint32_t addr, uint32_t lbo, uint
     return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(lbo >> 4) << 16 |
            static_cast<uint64_t>(sbo >> 4) << 32 | static_cast<uint64_t>(1) << 46;
 }
-// e4m3 A and B (both K-major), fp32 D, M x N.
-__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
-    return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+// e4m3 A, e4m3 or e5m2 B (both K-major), fp32 D, M x N.
+__host__ __device__ constexpr uint32_t idesc_8bit(int M, int N, bool e5m2_b) {
+    return (1u << 4) | (e5m2_b ? 1u << 10 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
-__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void mma_8bit(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
     asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
                  " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b),
                  "r"(idesc), "r"(acc ? 1u : 0u) : "memory");
 }
+// Two fp32 values rounded to e5m2 codes (nearest, ties to even; NaN stays), `lo` in the
+// low byte; and such codes as an f16 pair: an e5m2 code is the upper half of an f16.
+__device__ __forceinline__ uint32_t e5m2x2_from_f32(float lo, float hi) {
+    uint16_t y;
+    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(y) : "f"(hi), "f"(lo));
+    return y;
+}
+__device__ __forceinline__ uint32_t e5m2x2_to_f16x2(uint32_t two_codes) { return __byte_perm(two_codes, 0u, 0x1404); }
 // Four consecutive columns of this warp's lanes (the caller waits).
 __device__ __forceinline__ void tmem_ld4(uint32_t taddr, float (&v)[4]) {
     uint32_t r[4];
@@ -483,10 +507,10 @@ window_decode_kernel(const WindowParams p, int* counters, const __grid_constant_
         int votes = 0;
         float acc[C::kAddSteps ? GM : 4] = {};                     // kAddSteps: the item's steps before the last one
         auto add_parts = [&](const float (&o)[C::kPParts][4], int k) {
-            // (bf16 remainders have their own exponents; e4m3 ones were scaled by 16)
+            // (bf16 remainders have their own exponents; 8-bit ones were scaled)
             float y = 0.f;
 #pragma unroll
-            for (int i = C::kPParts - 1; i >= 0; --i) y = CODE ? fmaf(y, 1.f / 16, o[i][k]) : y + o[i][k];
+            for (int i = C::kPParts - 1; i >= 0; --i) y = CODE ? fmaf(y, 1.f / C::kPart, o[i][k]) : y + o[i][k];
             return y;
         };
         const int steps = n[grp];
@@ -610,10 +634,8 @@ window_decode_kernel(const WindowParams p, int* counters, const __grid_constant_
                     x[0][g] = seen ? x[0][g] : -INFINITY;          // (after the scaling: -inf times 0 is NaN)
                 }
                 // References, the same for the group's 128 tokens: raised when unset or
-                // passed by 2^8, of weights by 2^4 (codes: the largest weight is then
-                // 2^4 .. 2^8, inside e4m3's 448).  Usually none rises, which one vote and
-                // four flags tell; the maxima are formed only when one does.
-                constexpr float kLift = CODE ? 4.f : 0.f, kLag = CODE ? 4.f : 8.f;
+                // passed by 2^8, of codes' weights by 2^kLag.  Usually none rises, which one
+                // vote and four flags tell; the maxima are formed only when one does.
                 if (first) {
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
@@ -626,7 +648,7 @@ window_decode_kernel(const WindowParams p, int* counters, const __grid_constant_
                     bool need = false;
 #pragma unroll
                     for (int g = 0; g < 4; ++g)
-                        if (g0 + g < G) need |= x[0][g] > r_m[g] + 8.f || (CODE && x[0][g] + ev > r_o[g] + (kLift + kLag));
+                        if (g0 + g < G) need |= x[0][g] > r_m[g] + 8.f || (CODE && x[0][g] + ev > r_o[g] + (C::kLift + C::kLag));
                     const bool any = __any_sync(0xffffffffu, need);
                     // (a vote's flags are written again two votes on, past another barrier)
                     if (lane == 0) m.flags[grp][votes & 1][wq] = any;
@@ -687,8 +709,8 @@ window_decode_kernel(const WindowParams p, int* counters, const __grid_constant_
                                 r_m[g] = mx;
                                 l[g] *= old_m == -INFINITY ? 0.f : pa_dev::ex2(old_m - mx);
                             }
-                            if (mo - kLift > old_o + kLag) {
-                                r_o[g] = mo - kLift;
+                            if (mo - C::kLift > old_o + C::kLag) {
+                                r_o[g] = mo - C::kLift;
                                 if (old_o != -INFINITY) {
                                     corr[g] = pa_dev::ex2(old_o - r_o[g]);
                                     scale_o = true;
@@ -732,12 +754,12 @@ window_decode_kernel(const WindowParams p, int* counters, const __grid_constant_
 #pragma unroll
                     for (int g = 0; g < 4; g += 2) {
                         if constexpr (CODE) {
-                            const uint32_t c = pa_dev::e4m3x2_from_f32(v[g], v[g + 1]);
+                            const uint32_t c = C::kE5 ? e5m2x2_from_f32(v[g], v[g + 1]) : pa_dev::e4m3x2_from_f32(v[g], v[g + 1]);
                             pcol[g * 16] = static_cast<unsigned char>(c);
                             pcol[g * 16 + 16] = static_cast<unsigned char>(c >> 8);
-                            const uint32_t f = pa_dev::e4m3x2_to_f16x2(c);
-                            v[g] = (v[g] - pa_dev::f16_lo(f)) * 16.f;
-                            v[g + 1] = (v[g + 1] - pa_dev::f16_hi(f)) * 16.f;
+                            const uint32_t f = C::kE5 ? e5m2x2_to_f16x2(c) : pa_dev::e4m3x2_to_f16x2(c);
+                            v[g] = (v[g] - pa_dev::f16_lo(f)) * C::kPart;
+                            v[g + 1] = (v[g + 1] - pa_dev::f16_hi(f)) * C::kPart;
                         } else {
                             const uint32_t c = pa_dev::pack_bf16(v[g], v[g + 1]);
                             *reinterpret_cast<uint16_t*>(pcol + g * 16) = static_cast<uint16_t>(c);
@@ -972,8 +994,8 @@ window_decode_kernel(const WindowParams p, int* counters, const __grid_constant_
                 if constexpr (CODE) {
 #pragma unroll
                     for (int i = 0; i < kStep / 32; ++i)
-                        if (2 * i < blocks) mma_e4m3(o, plain_desc(v + i * 4096, 2048, 128), plain_desc(pt + i * 2 * kLbo, kLbo, 128),
-                                 idesc_e4m3(kD, C::kNP), !(first && i == 0));
+                        if (2 * i < blocks) mma_8bit(o, plain_desc(v + i * 4096, 2048, 128), plain_desc(pt + i * 2 * kLbo, kLbo, 128),
+                                 idesc_8bit(kD, C::kNP, C::kE5), !(first && i == 0));
                 } else {
 #pragma unroll
                     for (int i = 0; i < kStep / 16; ++i)
@@ -1008,8 +1030,8 @@ window_decode_kernel(const WindowParams p, int* counters, const __grid_constant_
                 if constexpr (CODE) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        mma_e4m3(tmem + sb * C::kNQ, pa_tc::sw128_desc(k + i * 32), pa_tc::sw128_desc(q + i * 32),
-                                 idesc_e4m3(kStep, C::kNQ), i > 0);
+                        mma_8bit(tmem + sb * C::kNQ, pa_tc::sw128_desc(k + i * 32), pa_tc::sw128_desc(q + i * 32),
+                                 idesc_8bit(kStep, C::kNQ, false), i > 0);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
