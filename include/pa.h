@@ -464,9 +464,15 @@ int pa_prefill(pa_pool *pool, const void *q, int num_tokens, int num_q_heads,
  * 16-byte-aligned out take the tcgen05 kernel (unless PA_OPT_PREFILL_KERNEL is
  * 1), every other call a plain one that is many times slower.
  * A bf16 output of the tcgen05 kernel weighs the values with weights rounded to
- * 16 bits, an fp32 output with a rounded part and its remainder.  The tensor
- * cores cut sums towards zero, so an fp32 output is too small by about 2^-29 of
- * itself per visible key (6e-5 at 30000 keys; the plain kernel's is not).
+ * the type of its products: bf16 on bf16 pools (8 significant bits, 2^-8; pa_prefill
+ * carries a remainder there too), f16 on code pools (2^-11, and 2^-34 of the largest
+ * weight times its block's value scale).  An fp32 output has a rounded part and its
+ * remainder (2^-16, and 2^-22 with the same 2^-34).  Queries on code pools are f16
+ * after a power of two for each row: exact down to 2^-24 of the row's largest
+ * element, off by at most 2^-32 of it below.
+ * The tensor
+ * cores cut sums towards zero, so an fp32 output is too small by about 2^-28 of
+ * itself per visible key (1e-4 at 30000 keys; the plain kernel's is not).
  * Bits at positions past the context, and at positions that no row of a tile
  * (256 rows of consecutive chunk tokens and heads) sees, never reach the output.
  * As with pa_prefill, a key or value that is not finite and that some row of the

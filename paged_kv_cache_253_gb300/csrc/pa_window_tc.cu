@@ -16,10 +16,16 @@
 // Code pools: the codes are widened to f16 (exact) into the layouts the MMAs
 // read, f16 MMAs.  Each query row is scaled by a power of two that puts its
 // largest element into [2^7, 2^8), so bf16 queries of any size are exact in f16
-// down to 2^-25 of the row's largest.  A block's key scale multiplies its
+// down to 2^-24 of the row's largest.  A block's key scale multiplies its
 // scores.  Its value scale multiplies the weights: w = 2^(x - m) * 2^ev, f16
-// relative to a reference of its own (the largest w so far), because blocks may
-// differ by more than f16 holds.
+// relative to a reference of its own, because blocks may differ by more than f16
+// holds.  The reference keeps the largest w at 2^9 .. 2^15, the upper end of f16:
+// small weights are what its range is needed for, since many of them may count as
+// much as the largest, or be all of the result where the largest one's value is
+// zero.  What f16 cuts off is then under 2^-34 of the largest per key (2^-25 with
+// the largest at 1 .. 2^8: of 131072 keys, weights of e^-17.6 all vanished).  A
+// reference that is raised sooner gives more, and more sums to scale: 16 chunks,
+// cold L2, 215 us with 1 .. 2^8, 219 now, 227 with 2^12 .. 2^15.
 //
 // Why this shape: one tile's QK^T and PV take the tensor cores while the other
 // tile's threads compute weights; four MMA-sized TMEM buffers (two S/P, two O)
@@ -66,6 +72,9 @@ constexpr uint32_t kCodeOff = kInfoOff + 256;             // code pools: a step'
 constexpr uint32_t kCodeBytes = 16384;
 constexpr uint32_t smem_bytes(bool code) { return kCodeOff + (code ? 2 * kCodeBytes : 0) + 1024; }   // + alignment slack
 constexpr int kTmemCols = 512;           // S/P of tile t at 128 t, O of tile t at 256 + 128 t
+// Code pools: the largest weight is 2^kLift when a reference is set, 2^(kLift + kLag)
+// when it is raised (f16 holds up to 2^16)
+constexpr float kLift = 9.f, kLag = 6.f;
 enum Bar { kQFull, kSFull0, kSFull1, kPFull0, kPFull1, kOFull, kDone, kPartFull0, kPartFull1, kCodeFull0, kCodeFull1, kCodeEmpty0, kCodeEmpty1, kKFull0, kKEmpty0 = kKFull0 + kStages,
            kVFull0 = kKEmpty0 + kStages, kVEmpty0 = kVFull0 + kStages, kNumBars = kVEmpty0 + kStages };
 // warps: 0-3 and 4-7 weights of tile 0 and 1, 8 copies, 9 MMA issue, 12-15 widening
@@ -411,8 +420,8 @@ window_prefill_kernel(const WindowParams p, const __grid_constant__ CUtensorMap 
                 if (old_m != -INFINITY) l *= pa_dev::ex2(old_m - mx);
             }
             const float oref_old = CODE ? o_ref : old_m;
-            const bool up_o = CODE ? mo > o_ref + 8.f : up;
-            if (CODE && up_o) o_ref = mo;
+            const bool up_o = CODE ? mo - kLift > o_ref + kLag : up;
+            if (CODE && up_o) o_ref = mo - kLift;
             const float oref_new = CODE ? o_ref : m_ref;
             if (__any_sync(0xffffffffu, up_o && oref_old != -INFINITY)) {
                 // O holds the sums of all earlier steps (S(j) is full: their MMAs are done)

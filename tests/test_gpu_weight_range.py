@@ -63,3 +63,22 @@ def test_decode_keeps_small_weights(kind, out_dtype, floor, many, at, gap, sprea
     out, tol = bound(q, k, v, torch.ones(1, n, dtype=torch.bool, device=DEV), out_dtype, floor)
     worst = ((got.double() - out).abs() / tol).amax((0, 2))
     assert (worst <= 1).all(), f"{worst.tolist()} times the bound (by head)"
+
+
+# 2^-25 of 2^9 at least; each product of 16 keys cuts the sum by less than 2^-23 of itself, and
+# fp32 results take two (a rounded part and a remainder)
+@pytest.mark.parametrize("kind", ["fp8", "fp8b", "bf16"])
+@pytest.mark.parametrize("out_dtype,cut", [(torch.bfloat16, 2.0 ** -27), (torch.float32, 2.0 ** -26)])
+@pytest.mark.parametrize("at,gap,spread", [(0, 17.0, 0.3), (0, 17.6, 0.1), (131068, 17.0, 0.3)])
+def test_prefill_keeps_small_weights(kind, out_dtype, cut, at, gap, spread):
+    n, T = 131072, 3
+    pool, k, v, t = heavy(kind, n, at, gap, spread, seed=int(gap * 2))
+    q = HEADS.to(DEV)[None, :, None].expand(T, 4, D).bfloat16().contiguous()
+    i32 = dict(dtype=torch.int32, device=DEV)
+    got = pool.prefill(q, torch.tensor([0, T], **i32), t, torch.tensor([n], **i32), 1 / math.sqrt(D), max_q_len=T,
+                       out_dtype=out_dtype, window=1 << 30)
+    assert pool.get_error() == 0
+    j, p = torch.arange(n, device=DEV)[None], torch.arange(n - T, n, device=DEV)[:, None]
+    out, tol = bound(q, k, v, j <= p, out_dtype, 2.0 ** -34, n * cut)
+    worst = ((got.double() - out).abs() / tol).amax((0, 2))
+    assert (worst <= 1).all(), f"{worst.tolist()} times the bound (by head)"
