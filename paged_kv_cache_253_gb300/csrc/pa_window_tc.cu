@@ -772,6 +772,10 @@ window_prefill_kernel(const WindowParams p, const __grid_constant__ CUtensorMap 
                 for (int b = 0; b < kStepBlks; ++b)
                     c[b] = (have >> b) & 1 ? *reinterpret_cast<const uint4*>(base + kCodeOff + which * kCodeBytes + b * 2048 + ct * 16)
                                            : make_uint4(0u, 0u, 0u, 0u);     // code 0 is +0
+                // the loads are done before the next copy, of another proxy, may write there: an
+                // arrival alone does not order them (beside slow loads and stores of the weight
+                // warps, some lanes then read the codes of the step after)
+                pa_tc::fence_smem_to_async();
                 __syncwarp();
                 if (lane == 0) arrive(&bars[kCodeEmpty0 + which]);
                 return true;
