@@ -470,9 +470,10 @@ int pa_prefill(pa_pool *pool, const void *q, int num_tokens, int num_q_heads,
  * remainder (2^-16, and 2^-22 with the same 2^-34).  Queries on code pools are f16
  * after a power of two for each row: exact down to 2^-24 of the row's largest
  * element, off by at most 2^-32 of it below.
- * The tensor
- * cores cut sums towards zero, so an fp32 output is too small by about 2^-28 of
- * itself per visible key (1e-4 at 30000 keys; the plain kernel's is not).
+ * The tensor cores cut sums towards zero, by under 2^-23 of themselves for every 16
+ * keys: a bf16 output's all along (2^-27 per visible key at most, 2^-29 as a rule), an
+ * fp32 output's two parts for 4096 keys at a time (2^-14 at most, 2^-16 as a rule, at
+ * any length), after which totals are added with rounding.
  * Bits at positions past the context, and at positions that no row of a tile
  * (256 rows of consecutive chunk tokens and heads) sees, never reach the output.
  * As with pa_prefill, a key or value that is not finite and that some row of the
