@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, ROPE ? 2 : 3) append_tile_kernel(con
             if constexpr (KIND == kScaled) {
                 asm volatile("redux.sync.max.f32 %0, %0, 0xffffffff;" : "+f"(amax));
                 const int b = max(b_old, scale_exponent(amax));
-                inv = pow2(254 - b);                                 // 2^(127 - b)
+                inv = pa_dev::inverse_scale(b);
                 rises = b != b_old;
                 shrink = b_old > 0 ? pow2(max(0, b_old - b + 127)) : 0.f;
                 if (lane == 0) p.scales[si] = static_cast<uint8_t>(b);

@@ -133,6 +133,12 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
     return y;
 }
 
+// 2^(127 - b), the inverse of a block scale with biased exponent b in [1, 254] (the last is a
+// subnormal number).
+__device__ __forceinline__ float inverse_scale(int b) {
+    return __uint_as_float(b < 254 ? static_cast<uint32_t>(254 - b) << 23 : 0x00400000u);
+}
+
 // 2^x (hardware approximation; exact 0 for -inf).
 __device__ __forceinline__ float ex2(float x) {
     float y;

@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kThreads) append_scaled_kernel(
         }
         __syncwarp();
         // the new rows over it
-        const float inv = pow2(254 - b);                         // 2^(127 - b)
+        const float inv = pa_dev::inverse_scale(b);
         for (unsigned long long left = m; left; left &= left - 1) {
             const int o = __ffsll(static_cast<long long>(left)) - 1;
             for (int u = lane; u < units; u += 32) {
