@@ -293,9 +293,10 @@ int ensure_tc(pa_pool* pool, int S) {
                 pa_detail::window_decode_tc_partials(pool) + pa_detail::window_decode_tc_counters(pool, S));
 }
 
-size_t generic_partials(const pa_pool* pool, int64_t items, int G) {
-    return static_cast<size_t>(std::max<int64_t>(items, 4LL * pool->num_sms)) * G * (pool->head_dim + 2) *
-           sizeof(float);
+// The plain decode's partials, whatever the batch: a batch is split into no more than four
+// ranges per SM (splits), and one that is not split has none.
+size_t generic_partials(const pa_pool* pool, int G) {
+    return 4 * static_cast<size_t>(pool->num_sms) * G * (pool->head_dim + 2) * sizeof(float);
 }
 
 void fill(const pa_pool* pool, int Hq, float scale, WindowParams* p) {
@@ -322,8 +323,7 @@ namespace pa_detail {
 
 int window_reserve(pa_pool* pool, int max_seqs, int max_q_heads) {
     if (max_q_heads / pool->kv_heads > kMaxG) return PA_ERR_UNSUPPORTED;
-    const int rc = ensure_partials(pool, generic_partials(pool, static_cast<int64_t>(max_seqs) * pool->kv_heads,
-                                                          max_q_heads / pool->kv_heads));
+    const int rc = ensure_partials(pool, generic_partials(pool, max_q_heads / pool->kv_heads));
     return rc == PA_OK ? ensure_tc(pool, max_seqs) : rc;
 }
 
@@ -353,7 +353,7 @@ int decode_window(pa_pool* pool, const void* q, int num_seqs, int num_q_heads, c
     const int64_t cap = static_cast<int64_t>(max_blocks_per_seq) * pool->block_size;
     p.nsplit = splits(pool, num_seqs, std::min<int64_t>(cap, static_cast<int64_t>(window) + sinks));
     if (p.nsplit > 1) {
-        const int rc = ensure_partials(pool, generic_partials(pool, 0, p.G));
+        const int rc = ensure_partials(pool, generic_partials(pool, p.G));
         if (rc != PA_OK) return rc;
         p.part = static_cast<float*>(pool->wws);
     }

@@ -41,3 +41,26 @@ def test_appends_to_blocks_of_the_largest_scales(B, D, T, rotate, exponent):
     assert pool.get_error() == 0
     m.same(pool)
     assert (pool_values(pool)[1].abs() == 448 * 2.0 ** (exponent - 127)).sum() >= 2
+
+
+@pytest.mark.parametrize("kind,window", [("bf16", True), ("fp8b", False), ("fp8b", True)])
+def test_a_reserve_takes_what_a_call_uses(kind, window):
+    """The windowed decodes' workspace: partials by the GPU's size (some 5 MB for each of the two
+    kernels, with 16 heads a group) and four bytes per sequence and KV head; a batch of that many
+    sequences then runs without more."""
+    pool = KVPool(64, 16, 8, 128, kind, DEV)
+    torch.cuda.synchronize()
+    free = torch.cuda.mem_get_info()[0]
+    pool.reserve(16384, 128, window=window)
+    assert free - torch.cuda.mem_get_info()[0] <= 64 << 20
+    S = 2048
+    q = torch.randn(S, 128, 128, device=DEV).bfloat16()
+    t = torch.zeros(S, 1, dtype=torch.int32, device=DEV)
+    lens = torch.full((S,), 5, dtype=torch.int32, device=DEV)
+    out = torch.empty(S, 128, 128, device=DEV)
+    free = torch.cuda.mem_get_info()[0]
+    for o in (out, torch.empty(out.numel() + 1, device=DEV)[1:].view(out.shape)):        # (the plain kernel: unaligned)
+        free = torch.cuda.mem_get_info()[0]
+        pool.decode(q, t, lens, 0.1, out=o, window=9)
+        assert torch.cuda.mem_get_info()[0] == free and pool.get_error() == 0
+        assert not o.any()                                                               # an empty cache
