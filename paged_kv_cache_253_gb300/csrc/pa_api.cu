@@ -96,9 +96,6 @@ int pa_pool_create(int num_blocks, int block_size, int kv_heads, int head_dim, p
         static_cast<size_t>(num_blocks) * kv_heads * block_size * head_dim * elem_size(dtype);
     const size_t nb = static_cast<size_t>(num_blocks);
     const size_t scale_bytes = nb * kv_heads * 2, mask_bytes = nb * sizeof(unsigned long long);
-    // appends by block (block-scaled pools, and rotary ones of 16-token blocks) note a
-    // call's blocks there: 72 bytes per block of 16
-    const bool notes = scaled || (block_size == 16 && dtype != PA_F32);
     auto release = [p] {
         cudaFree(p->k);
         cudaFree(p->v);
@@ -111,9 +108,9 @@ int pa_pool_create(int num_blocks, int block_size, int kv_heads, int head_dim, p
     if (cudaMalloc(&p->k, bytes) != cudaSuccess || cudaMalloc(&p->v, bytes) != cudaSuccess ||
         cudaMalloc(reinterpret_cast<void**>(&p->err), sizeof(int)) != cudaSuccess ||
         (scaled && cudaMalloc(reinterpret_cast<void**>(&p->scales), scale_bytes) != cudaSuccess) ||
-        (notes && (cudaMalloc(reinterpret_cast<void**>(&p->app_mask), mask_bytes) != cudaSuccess ||
-                   cudaMalloc(reinterpret_cast<void**>(&p->app_token),
-                              nb * block_size * sizeof(int32_t)) != cudaSuccess))) {
+        (scaled && (cudaMalloc(reinterpret_cast<void**>(&p->app_mask), mask_bytes) != cudaSuccess ||
+                    cudaMalloc(reinterpret_cast<void**>(&p->app_token),
+                               nb * block_size * sizeof(int32_t)) != cudaSuccess))) {
         cudaGetLastError();
         release();
         return PA_ERR_OUT_OF_MEMORY;
@@ -121,7 +118,7 @@ int pa_pool_create(int num_blocks, int block_size, int kv_heads, int head_dim, p
     if (cudaMemset(p->k, 0, bytes) != cudaSuccess || cudaMemset(p->v, 0, bytes) != cudaSuccess ||
         cudaMemset(p->err, 0, sizeof(int)) != cudaSuccess ||
         (scaled && cudaMemset(p->scales, 0, scale_bytes) != cudaSuccess) ||
-        (notes && cudaMemset(p->app_mask, 0, mask_bytes) != cudaSuccess) ||
+        (scaled && cudaMemset(p->app_mask, 0, mask_bytes) != cudaSuccess) ||
         cudaDeviceSynchronize() != cudaSuccess) {
         release();
         return PA_ERR_CUDA;

@@ -26,8 +26,8 @@ struct pa_pool {
     // block-scaled pools (PA_FP8E4M3_BLOCK): biased exponents [num_blocks][kv_heads][2] (K, V)
     uint8_t* scales = nullptr;
     // scratch of appends by block: which offsets of a block the call writes (all zero
-    // between calls) and the token that writes each (block-scaled pools, and pools of
-    // 16-token blocks)
+    // between calls) and the token that writes each: 72 bytes per block of 16.  Block-scaled
+    // pools have it from the start, others from their first rotary append that needs it
     unsigned long long* app_mask = nullptr;     // [num_blocks]
     int32_t* app_token = nullptr;               // [num_blocks][block_size]
     // windowed attention's partials; outgrown buffers live until the pool is
@@ -252,6 +252,7 @@ int launch_append_notes(pa_pool* p, const int64_t* slots, int T, cudaStream_t st
 // Appends by whole block tiles (16-token blocks, head width 128), every pool type
 // but f32, and the read-back of such pools (pa_append_tile.cu).
 bool append_tile_eligible(const pa_pool* p, const void* k, const void* v, const RopeParams& r);
+bool append_notes_ready(pa_pool* p, int T, cudaStream_t st);     // its scratch for T tokens is there (made if need be)
 int launch_append_tile(pa_pool* p, const void* k, const void* v, const int64_t* slots, int T,
                        const RopeParams& rope, cudaStream_t st);
 bool read_tile_eligible(const pa_pool* p, const void* k, const void* v);

@@ -1,9 +1,12 @@
 """Block-scaled, windowed and rotary operators at the limits of what they are given: the
 largest scales, reserved workspaces, scratch, and calls that are refused before they have
 done anything."""
+import gc
+
 import pytest
 import torch
 
+import plain64
 from paged_kv_cache_253_gb300 import _lib as L
 from paged_kv_cache_253_gb300.api import KVPool
 from test_gpu_block_scaled import Model, pool_values
@@ -64,3 +67,51 @@ def test_a_reserve_takes_what_a_call_uses(kind, window):
         pool.decode(q, t, lens, 0.1, out=o, window=9)
         assert torch.cuda.mem_get_info()[0] == free and pool.get_error() == 0
         assert not o.any()                                                               # an empty cache
+
+
+@pytest.mark.parametrize("kind,es", [("bf16", 2), ("fp8", 1)])
+def test_pools_without_block_scales_hold_no_scratch(kind, es):
+    """Keys and values alone, up to the allocator's pages."""
+    nb, D = 1 << 20, 4
+    gc.collect()
+    torch.cuda.synchronize()
+    free = torch.cuda.mem_get_info()[0]
+    pool = KVPool(nb, 16, 1, D, kind, DEV)
+    assert free - torch.cuda.mem_get_info()[0] <= 2 * nb * 16 * D * es + (16 << 20)
+    pool.close()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+def test_a_first_rotary_append_inside_a_capture(kind):
+    """More tokens than a call searches by itself, first captured and replayed, then called: the
+    rows are the formula's either way."""
+    g = torch.Generator().manual_seed(5)
+    T, H, Hq, D = 700, 2, 4, 128
+    pool = KVPool(60, 16, H, D, kind, DEV)
+    if kind == "fp8":
+        pool.set_kv_scales(2.0 ** -5, 2.0 ** -5)
+    q, k, v = (torch.randn(T, h, D, generator=g).bfloat16().to(DEV) for h in (Hq, H, H))
+    slots = torch.randperm(60 * 16, generator=g)[:T].to(DEV)
+    pos = torch.randint(0, 100000, (T,), generator=g, dtype=torch.int32).to(DEV)
+    inv = (1e4 ** (-torch.arange(64, dtype=torch.float64) / 64)).float().to(DEV)
+    out = torch.zeros_like(q)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pool.append_rope(q, k, v, slots, pos, inv, q_out=out)
+    want_q, want_k = (plain64.rotate(x.cpu(), pos[None].cpu(), inv.cpu(), torch.zeros(64), False) for x in (q, k))
+    for call in (graph.replay, lambda: pool.append_rope(q, k, v, slots, pos, inv, q_out=out), graph.replay):
+        out.zero_()
+        pool.import_(*(torch.zeros_like(x) for x in pool.export()))
+        call()
+        kk, vv = (x.cpu().double() for x in pool.read_kv(slots))
+        # one rounding to bf16, and 2^-20 of the pair's length for the rotation in 32 bits; codes:
+        # half a step of e4m3, 2^-4 of the value or 2^-10 of the scale
+        r = 2.0 ** -20 * 8
+        assert ((out.cpu().double() - want_q).abs() <= 2.0 ** -8 * want_q.abs() + r).all()
+        if kind == "bf16":
+            assert ((kk - want_k).abs() <= 2.0 ** -8 * want_k.abs() + r).all() and torch.equal(vv, v.cpu().double())
+        else:
+            assert ((kk - want_k).abs() <= 2.0 ** -4 * want_k.abs() + 2.0 ** -15 + 2 * r).all()
+            assert ((vv - v.cpu().double()).abs() <= 2.0 ** -4 * v.cpu().double().abs() + 2.0 ** -15).all()
+    assert pool.get_error() == 0
