@@ -347,7 +347,10 @@ static int decode_impl(pa_pool* pool, const void* q, int num_seqs, int num_q_hea
     DeviceGuard g(pool->device);
     if (!g.ok) return PA_ERR_CUDA;
     if (pool->scales) {                            // the windowed kernels with no window
-        if (nt) {
+        if (nt) {                                  // (nothing is appended by a call that is refused)
+            rc = pa_detail::check_decode_window(pool, q, num_seqs, num_q_heads, block_tables, max_blocks_per_seq,
+                                                context_lens, kNoWindow, 0, out, out_dtype);
+            if (rc != PA_OK) return rc;
             rc = pa_append_kv(pool, nt->k, nt->v, nt->slots, num_seqs, stream);
             if (rc != PA_OK) return rc;
         }

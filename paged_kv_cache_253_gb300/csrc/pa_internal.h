@@ -258,7 +258,12 @@ int launch_append_tile(pa_pool* p, const void* k, const void* v, const int64_t* 
 bool read_tile_eligible(const pa_pool* p, const void* k, const void* v);
 int launch_read_tile(pa_pool* p, const int64_t* slots, int n, void* k, void* v, cudaStream_t st);
 
-// Windowed attention: generic kernel for every shape and pool type.
+// Windowed attention: generic kernel for every shape and pool type.  check_decode_window
+// is what decode_window checks and allocates before it launches.
+int check_decode_window(pa_pool* pool, const void* q, int num_seqs, int num_q_heads,
+                        const int32_t* block_tables, int max_blocks_per_seq,
+                        const int32_t* context_lens, int window, int sinks, void* out,
+                        pa_dtype out_dtype);
 int decode_window(pa_pool* pool, const void* q, int num_seqs, int num_q_heads,
                   const int32_t* block_tables, int max_blocks_per_seq,
                   const int32_t* context_lens, int window, int sinks, float scale, void* out,

@@ -327,11 +327,12 @@ int window_reserve(pa_pool* pool, int max_seqs, int max_q_heads) {
     return rc == PA_OK ? ensure_tc(pool, max_seqs) : rc;
 }
 
-int decode_window(pa_pool* pool, const void* q, int num_seqs, int num_q_heads, const int32_t* block_tables,
-                  int max_blocks_per_seq, const int32_t* context_lens, int window, int sinks, float scale, void* out,
-                  pa_dtype out_dtype, cudaStream_t st) {
+// Everything of a windowed decode that can fail before a launch: its arguments, its workspace.
+static int plan_decode_window(pa_pool* pool, const void* q, int num_seqs, int num_q_heads, const int32_t* block_tables,
+                              int max_blocks_per_seq, const int32_t* context_lens, int window, int sinks, float scale,
+                              void* out, pa_dtype out_dtype, WindowParams* params, bool* tc) {
     if (reinterpret_cast<uintptr_t>(out) % (out_dtype == PA_BF16 ? 2 : 4) != 0) return PA_ERR_INVALID_ARG;
-    WindowParams p{};
+    WindowParams& p = *params;
     fill(pool, num_q_heads, scale, &p);
     p.q = q;
     p.tables = block_tables;
@@ -343,12 +344,11 @@ int decode_window(pa_pool* pool, const void* q, int num_seqs, int num_q_heads, c
     p.window = std::min(window, 1 << 30);
     p.sinks = std::min(sinks, 1 << 30);
     p.out_bf16 = out_dtype == PA_BF16;
-    if (window_decode_tc_eligible(pool, p)) {
+    *tc = window_decode_tc_eligible(pool, p);
+    if (*tc) {
         const int rc = ensure_tc(pool, num_seqs);
-        if (rc != PA_OK) return rc;
         p.part = static_cast<float*>(pool->wtc);
-        return launch_window_decode_tc(
-            pool, p, reinterpret_cast<int*>(static_cast<char*>(pool->wtc) + window_decode_tc_partials(pool)), st);
+        return rc;
     }
     const int64_t cap = static_cast<int64_t>(max_blocks_per_seq) * pool->block_size;
     p.nsplit = splits(pool, num_seqs, std::min<int64_t>(cap, static_cast<int64_t>(window) + sinks));
@@ -357,6 +357,29 @@ int decode_window(pa_pool* pool, const void* q, int num_seqs, int num_q_heads, c
         if (rc != PA_OK) return rc;
         p.part = static_cast<float*>(pool->wws);
     }
+    return PA_OK;
+}
+
+int check_decode_window(pa_pool* pool, const void* q, int num_seqs, int num_q_heads, const int32_t* block_tables,
+                        int max_blocks_per_seq, const int32_t* context_lens, int window, int sinks, void* out,
+                        pa_dtype out_dtype) {
+    WindowParams p{};
+    bool tc;
+    return plan_decode_window(pool, q, num_seqs, num_q_heads, block_tables, max_blocks_per_seq, context_lens, window,
+                              sinks, 1.f, out, out_dtype, &p, &tc);
+}
+
+int decode_window(pa_pool* pool, const void* q, int num_seqs, int num_q_heads, const int32_t* block_tables,
+                  int max_blocks_per_seq, const int32_t* context_lens, int window, int sinks, float scale, void* out,
+                  pa_dtype out_dtype, cudaStream_t st) {
+    WindowParams p{};
+    bool tc;
+    const int rc = plan_decode_window(pool, q, num_seqs, num_q_heads, block_tables, max_blocks_per_seq, context_lens,
+                                      window, sinks, scale, out, out_dtype, &p, &tc);
+    if (rc != PA_OK) return rc;
+    if (tc)
+        return launch_window_decode_tc(
+            pool, p, reinterpret_cast<int*>(static_cast<char*>(pool->wtc) + window_decode_tc_partials(pool)), st);
     cudaError_t e = launch_any(pool, p, dim3(num_seqs * p.nsplit, p.Hkv), st);
     if (e == cudaSuccess && p.nsplit > 1) {
         e = launch_pdl(window_merge_kernel, dim3(num_seqs * p.Hkv), dim3(kThreads), 0, st, p);

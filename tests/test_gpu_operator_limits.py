@@ -115,3 +115,19 @@ def test_a_first_rotary_append_inside_a_capture(kind):
             assert ((kk - want_k).abs() <= 2.0 ** -4 * want_k.abs() + 2.0 ** -15 + 2 * r).all()
             assert ((vv - v.cpu().double()).abs() <= 2.0 ** -4 * v.cpu().double().abs() + 2.0 ** -15).all()
     assert pool.get_error() == 0
+
+
+@pytest.mark.parametrize("B", [16, 32])
+def test_a_refused_append_decode_appends_nothing(B):
+    """Block-scaled pools append, then decode: an output that the decode refuses is refused before."""
+    pool = KVPool(4, B, 2, 128, "fp8b", DEV)
+    k, q = torch.randn(1, 2, 128, device=DEV).bfloat16(), torch.randn(1, 8, 128, device=DEV).bfloat16()
+    slot, out = torch.zeros(1, dtype=torch.int64, device=DEV), torch.full((1100,), 7.0, device=DEV)
+    t, lens = torch.zeros(1, 1, dtype=torch.int32, device=DEV), torch.ones(1, dtype=torch.int32, device=DEV)
+    args = (pool.handle, k.data_ptr(), k.data_ptr(), slot.data_ptr(), q.data_ptr(), 1, 8, t.data_ptr(), 1, lens.data_ptr(), 0.1)
+    assert L.pa_append_decode(*args, out.data_ptr() + 2, L.PA_F32, None) == L.PA_ERR_INVALID_ARG
+    assert L.pa_append_decode(*args, out.data_ptr() + 1, L.PA_BF16, None) == L.PA_ERR_INVALID_ARG
+    torch.cuda.synchronize()
+    assert not pool.export()[0].any() and not pool.export_scales().any() and (out == 7).all()
+    assert L.pa_append_decode(*args, out.data_ptr(), L.PA_F32, None) == 0 and pool.get_error() == 0
+    assert pool.export()[0].any() and (out[:1024] != 7).all() and (out[1024:] == 7).all()
