@@ -15,8 +15,9 @@
  *     such code in the pool's device error word; pa_get_error reports it.
  *     No call traps or aborts.
  *   - Device pointers: every tensor argument marked "device" is GPU memory
- *     owned by the caller, on the device the pool was created on.  The
- *     library never frees caller memory.
+ *     owned by the caller, on the device the pool was created on, and aligned
+ *     to its elements (the attention calls' q to 16 bytes; else
+ *     PA_ERR_INVALID_ARG).  The library never frees caller memory.
  *   - Streams: `stream` is a cudaStream_t passed as void*.  NULL means the
  *     legacy default stream.  Every GPU call is asynchronous on it.
  *   - CUDA graphs: once the pool's workspace holds the batch (a first call of

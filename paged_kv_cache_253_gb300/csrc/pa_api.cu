@@ -259,7 +259,9 @@ int pa_append_kv(pa_pool* pool, const void* k, const void* v, const int64_t* slo
                  int num_tokens, void* stream) {
     if (!pool || num_tokens < 0) return PA_ERR_INVALID_ARG;
     if (num_tokens == 0) return PA_OK;
-    if (!k || !v || !slot_mapping || !aligned(slot_mapping, 8)) return PA_ERR_INVALID_ARG;
+    const size_t es = pool->dtype == PA_F32 ? 4 : 2;             // k and v elements
+    if (!k || !v || !slot_mapping || !aligned(slot_mapping, 8) || !aligned(k, es) || !aligned(v, es))
+        return PA_ERR_INVALID_ARG;
     if (static_cast<int64_t>(num_tokens) * pool->kv_heads * 32 > (int64_t{1} << 31) * 256)
         return PA_ERR_UNSUPPORTED;
     DeviceGuard g(pool->device);
@@ -295,7 +297,9 @@ int check_decode_args(const pa_pool* pool, const void* q, int S, int Hq, const i
     if (S > 16384) return PA_ERR_UNSUPPORTED;
     if (S == 0) return PA_OK;
     if (!q || !tables || !lens || !out || max_blocks == 0) return PA_ERR_INVALID_ARG;
-    if (!aligned(q, 16)) return PA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(tables, 4) || !aligned(lens, 4) ||
+        !aligned(out, out_dtype == PA_BF16 ? 2 : 4))
+        return PA_ERR_INVALID_ARG;
     if (static_cast<int64_t>(max_blocks) * pool->block_size > (int64_t{1} << 30))
         return PA_ERR_UNSUPPORTED;
     return PA_OK;

@@ -374,7 +374,9 @@ extern "C" int pa_prefill(pa_pool* pool, const void* q, int num_tokens, int num_
     if (num_seqs == 0 || num_tokens == 0 || max_q_len == 0) return PA_OK;
     if (!q || !cu_seqlens_q || !block_tables || !context_lens || !out || max_blocks_per_seq == 0)
         return PA_ERR_INVALID_ARG;
-    if (reinterpret_cast<uintptr_t>(q) % 16 != 0 || reinterpret_cast<uintptr_t>(out) % 8 != 0)
+    if (reinterpret_cast<uintptr_t>(q) % 16 != 0 || reinterpret_cast<uintptr_t>(out) % 8 != 0 ||
+        (reinterpret_cast<uintptr_t>(cu_seqlens_q) | reinterpret_cast<uintptr_t>(block_tables) |
+         reinterpret_cast<uintptr_t>(context_lens)) % 4 != 0)
         return PA_ERR_INVALID_ARG;
     if (static_cast<int64_t>(max_blocks_per_seq) * B > (int64_t{1} << 30)) return PA_ERR_UNSUPPORTED;
     const int G = num_q_heads / Hkv;

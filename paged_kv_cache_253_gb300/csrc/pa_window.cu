@@ -24,6 +24,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kKeys = 128;           // keys per chunk
+bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 constexpr int kMaxG = 16;
 
 __device__ __forceinline__ float elem(const float* p) { return __ldg(p); }
@@ -331,7 +332,6 @@ int window_reserve(pa_pool* pool, int max_seqs, int max_q_heads) {
 static int plan_decode_window(pa_pool* pool, const void* q, int num_seqs, int num_q_heads, const int32_t* block_tables,
                               int max_blocks_per_seq, const int32_t* context_lens, int window, int sinks, float scale,
                               void* out, pa_dtype out_dtype, WindowParams* params, bool* tc) {
-    if (reinterpret_cast<uintptr_t>(out) % (out_dtype == PA_BF16 ? 2 : 4) != 0) return PA_ERR_INVALID_ARG;
     WindowParams& p = *params;
     fill(pool, num_q_heads, scale, &p);
     p.q = q;
@@ -428,7 +428,8 @@ extern "C" int pa_prefill_window(pa_pool* pool, const void* q, int num_tokens, i
     if (num_seqs == 0 || num_tokens == 0 || max_q_len == 0) return PA_OK;
     const size_t osz = out_dtype == PA_BF16 ? 2 : 4;
     if (!q || !cu_seqlens_q || !block_tables || !context_lens || !out || max_blocks_per_seq == 0 ||
-        reinterpret_cast<uintptr_t>(q) % 16 != 0 || reinterpret_cast<uintptr_t>(out) % osz != 0)
+        !aligned(q, 16) || !aligned(out, osz) || !aligned(cu_seqlens_q, 4) || !aligned(block_tables, 4) ||
+        !aligned(context_lens, 4))
         return PA_ERR_INVALID_ARG;
     if (static_cast<int64_t>(max_blocks_per_seq) * pool->block_size > (int64_t{1} << 30)) return PA_ERR_UNSUPPORTED;
     pa_detail::DeviceGuard g(pool->device);

@@ -131,3 +131,25 @@ def test_a_refused_append_decode_appends_nothing(B):
     assert not pool.export()[0].any() and not pool.export_scales().any() and (out == 7).all()
     assert L.pa_append_decode(*args, out.data_ptr(), L.PA_F32, None) == 0 and pool.get_error() == 0
     assert pool.export()[0].any() and (out[:1024] != 7).all() and (out[1024:] == 7).all()
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "fp8", "fp8b"])
+def test_pointers_that_are_not_aligned_to_their_elements_are_refused(kind):
+    """By the host, before anything is launched; k, v and outputs at half an element, tables and
+    lengths at half an int."""
+    pool = KVPool(4, 16, 2, 128, kind, DEV)
+    buf = torch.zeros(64 * 1024, dtype=torch.uint8, device=DEV)
+    a, half = buf.data_ptr(), 2 if kind == "f32" else 1
+    for k, v, s in ((a + half, a, a), (a, a + half, a), (a, a, a + 4)):
+        assert L.pa_append_kv(pool.handle, k, v, s, 1, None) == L.PA_ERR_INVALID_ARG
+        assert L.pa_append_rope(pool.handle, None, 0, 0, k, 256, v, 256, s, 1, a, 1, a, None, 128, 0, None, None) \
+            == L.PA_ERR_INVALID_ARG
+        assert L.pa_read_kv(pool.handle, s, 1, k, v, None) == L.PA_ERR_INVALID_ARG
+    for t, n, o, dt in ((a + 2, a, a, L.PA_F32), (a, a + 2, a, L.PA_F32), (a, a, a + 2, L.PA_F32), (a, a, a + 1, L.PA_BF16)):
+        assert L.pa_decode_window(pool.handle, a, 1, 8, t, 1, n, 9, 0, 0.1, o, dt, None) == L.PA_ERR_INVALID_ARG
+        assert L.pa_decode(pool.handle, a, 1, 8, t, 1, n, 0.1, o, dt, None) == L.PA_ERR_INVALID_ARG
+        assert L.pa_prefill_window(pool.handle, a, 1, 8, a, 1, 1, t, 1, n, 9, 0, 0.1, o, dt, None) == L.PA_ERR_INVALID_ARG
+        if kind in ("bf16", "fp8", "fp8b"):
+            assert L.pa_prefill(pool.handle, a, 1, 8, a, 1, 1, t, 1, n, 0.1, o, dt, None) == L.PA_ERR_INVALID_ARG
+    assert L.pa_prefill_window(pool.handle, a, 1, 8, a + 2, 1, 1, a, 1, a, 9, 0, 0.1, a, L.PA_F32, None) == L.PA_ERR_INVALID_ARG
+    assert pool.get_error() == 0 and not pool.export()[0].any()
