@@ -43,8 +43,9 @@ def _dev(t, dtype, name, device):
 
 
 def _span(x):
-    """A count of positions for a C int: no context reaches beyond 2^30."""
-    return min(int(x), 1 << 30)
+    """A count of positions for a C int: no context reaches beyond 2^30, and a negative
+    one (refused there) stays negative."""
+    return max(min(int(x), 1 << 30), -(1 << 31))
 
 
 def _i32p(a):

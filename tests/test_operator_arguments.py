@@ -1,0 +1,21 @@
+"""Arguments that the Python calls turn into C ones: none becomes another value on the way,
+none of the wrong shape is taken for a part of itself.  No GPU is needed."""
+import pytest
+import torch
+
+from paged_kv_cache_253_gb300 import api
+
+NO_GPU = torch.device("cpu")
+
+
+def bare_pool():
+    pool = api.KVPool.__new__(api.KVPool)
+    pool.device, pool.dtype, pool.handle = NO_GPU, torch.bfloat16, None
+    pool.kv_heads, pool.head_dim = 2, 128
+    return pool
+
+
+@pytest.mark.parametrize("x", [-1, -(1 << 31), -(1 << 31) - 1, -(1 << 32) + 5, -(1 << 40), -(1 << 64) + 9])
+def test_negative_counts_stay_negative_as_c_ints(x):
+    import ctypes
+    assert ctypes.c_int(api._span(x)).value < 0
