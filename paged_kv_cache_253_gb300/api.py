@@ -139,6 +139,8 @@ class KVPool:
         the axis of each pair, all 0 when not given.  q, k and v may be slices of
         one projection's output: only a token's heads have to be contiguous.
         q None: keys and values only, returns None."""
+        if slot_mapping.dim() != 1:
+            raise ValueError("slot_mapping must be [T]")
         T, hkv, d = slot_mapping.shape[0], self.kv_heads, self.head_dim
         if k.shape != (T, hkv, d) or v.shape != (T, hkv, d):
             raise ValueError(f"k/v must be {(T, hkv, d)}")
@@ -192,6 +194,8 @@ class KVPool:
 
     def read_kv(self, slots):
         """(k, v), [n, Hkv, D] each, of the tokens stored at slots (int64 [n])."""
+        if slots.dim() != 1:
+            raise ValueError("slots must be [n]")
         n = slots.shape[0]
         k = torch.empty((n, self.kv_heads, self.head_dim), dtype=self.dtype, device=self.device)
         v = torch.empty_like(k)

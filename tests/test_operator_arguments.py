@@ -19,3 +19,14 @@ def bare_pool():
 def test_negative_counts_stay_negative_as_c_ints(x):
     import ctypes
     assert ctypes.c_int(api._span(x)).value < 0
+
+
+def test_slots_are_one_list():
+    """A table of slots is not read as its first row's worth."""
+    pool, k = bare_pool(), torch.zeros(3, 2, 128, dtype=torch.bfloat16)
+    pos, inv = torch.zeros(3, dtype=torch.int32), torch.ones(64)
+    for slots in (torch.zeros(3, 2, dtype=torch.int64), torch.zeros(3, 1, dtype=torch.int64), torch.tensor(3)):
+        with pytest.raises(ValueError):
+            pool.read_kv(slots)
+        with pytest.raises(ValueError):
+            pool.append_rope(None, k, k, slots, pos, inv)
