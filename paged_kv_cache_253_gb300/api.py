@@ -21,11 +21,15 @@ _CODE = {torch.float32: L.PA_F32, torch.bfloat16: L.PA_BF16, "f32": L.PA_F32,
 _OUT = {torch.float32: L.PA_F32, torch.bfloat16: L.PA_BF16}
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# torch's own query for a raw handle: 0.1 us, where the public one takes 2 us of a call's 4 to
+# 12.  It is no public name, so a torch without it is asked the public way.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(device):
     """The current stream of `device`, as a raw handle."""
+    if _raw_stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
     return _raw_stream(device.index)
 
 

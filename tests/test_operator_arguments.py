@@ -30,3 +30,28 @@ def test_slots_are_one_list():
             pool.read_kv(slots)
         with pytest.raises(ValueError):
             pool.append_rope(None, k, k, slots, pos, inv)
+
+
+def test_the_front_end_does_without_private_torch_names():
+    """A torch whose private stream query is gone (or a build without CUDA, which has none) still
+    imports the front end, which then asks for streams the public way."""
+    import subprocess
+    import sys
+    code = ("import torch\n"
+            "for n in ('_cuda_getCurrentRawStream', '_cuda_getCurrentStream'):\n"
+            "    if hasattr(torch._C, n): delattr(torch._C, n)\n"
+            "import paged_kv_cache_253_gb300.api as a\n"
+            "print(a.fnv1a64(b''))\n")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+
+
+@pytest.mark.gpu
+def test_streams_are_the_same_either_way(monkeypatch):
+    dev, st = torch.device("cuda", torch.cuda.current_device()), torch.cuda.Stream()
+    for use in (torch.cuda.current_stream(), st):
+        with torch.cuda.stream(use):
+            fast = api._stream(dev)
+            monkeypatch.setattr(api, "_raw_stream", None)
+            assert api._stream(dev) == fast == use.cuda_stream
+            monkeypatch.undo()
