@@ -336,6 +336,11 @@ int pa_decode_reserve(pa_pool *pool, int max_seqs, int max_q_heads);
  * out; bf16 pools 2^-16) or 2^-20 (fp32 out) of itself, and on code pools by
  * 2^-38 (bf16 out) or 2^-32 (fp32 out) of the largest weight, a weight being the
  * key's times its block's value scale.
+ * The tensor cores cut sums towards zero, by under 2^-23 of themselves with every
+ * product of 16 keys (32 on code pools).  fp32 results are therefore added up outside,
+ * on bf16 pools step by step (1e-6 of the result in all), on code pools every 8192 keys
+ * (2^-15 at most, 2^-17 as a rule, at any length); bf16 results are not (2^-27 per key
+ * at most, 2^-29 as a rule, of the keys of one sequence that one CTA walks).
  * Workspace: partials of split contexts, grown on demand (cudaMalloc);
  * pa_decode_window_reserve sizes it ahead of time, for any window (for a
  * PA_FP8E4M3_BLOCK pool, pa_decode_reserve does).  Calls on one pool must not

@@ -84,6 +84,8 @@ enum Bar { kQFull0, kQEmpty0 = kQFull0 + 4, kSFull0 = kQEmpty0 + 4, kSEmpty0 = k
 // one barrier for both, a group could ask for its own copy while the other's, in the
 // phase before, is still under way, and be told that it has landed.
 
+constexpr int kSlot = kMaxG * (kD + 4);       // floats of a partial: sums, then (reference, sum of weights, weights' reference)
+constexpr int kChunk = 64;                   // steps of a chunk (see Cfg)
 constexpr int kInfo = 16;                    // steps whose description is kept
 
 // The small things behind the operands.
@@ -117,7 +119,7 @@ struct Misc {
 // Everything that follows from the template arguments.  GM: 4, 8 or 16, at
 // least the query heads per KV head.  Column part * GM + g of an N side holds
 // part `part` of head g.
-template <bool CODE, bool WIDE, int GM>      // WIDE: fp32 output
+template <bool CODE, bool WIDE, int GM, bool CHUNKS = false>      // WIDE: fp32 output
 struct Cfg {
     static constexpr int kQParts = CODE ? 3 : 1;
     static constexpr int kPParts = CODE ? (WIDE ? 5 : 4) : (WIDE ? 3 : 2);
@@ -127,10 +129,16 @@ struct Cfg {
     static constexpr bool kE5 = CODE && !WIDE;
     static constexpr float kPart = kE5 ? 8.f : 16.f;
     static constexpr float kLift = !CODE ? 0.f : WIDE ? 6.f : 12.f, kLag = !CODE ? 8.f : WIDE ? 2.5f : 3.f;
-    // The tensor cores cut a sum to fp32 after each 16 keys, always towards zero: over
-    // 30000 bf16 keys that made a result 1e-5 smaller than it is.  For fp32 outputs each
-    // step's product starts from zero and the steps are added in registers, rounded to
-    // nearest.  (Sums of products of codes have few bits: 4e-7 over the same length.)
+    // The tensor cores cut a sum to fp32 after each 16 keys (32 of codes), always towards
+    // zero: over 30000 bf16 keys that made a result 1e-5 smaller than it is, over 131072 of
+    // codes in one range up to 3e-4.  For fp32 results of bf16 pools each step's product
+    // starts from zero and the steps are added in registers, rounded to nearest.  For fp32
+    // results of code pools, whose products have fewer bits, an item of many steps is walked
+    // in chunks of kChunk, which are joined like the parts of an item that several groups
+    // share.  That is a kernel of its own: whatever makes the code longer costs the others
+    // (8 sequences of 32768 .. 131072, fp32: 213 us without chunks, 225 with; sums in
+    // registers or added to memory step by step cost all of them 12 to 38 % from eight
+    // heads a group on).
     static constexpr bool kAddSteps = WIDE && !CODE;
     static constexpr int kNQ = (kQParts * GM + 15) / 16 * 16;
     static constexpr int kNP = (kPParts * GM + 15) / 16 * 16;
@@ -279,7 +287,7 @@ __device__ __forceinline__ void merge_item(const WindowParams& p, long long c_fi
     for (int qd = gt; qd < p.G * (kD / 4); qd += 128) {
         const int g = qd / (kD / 4), d = qd % (kD / 4) * 4;
         auto part = [&](int i) {
-            return p.part + (2 * static_cast<size_t>(c_first + i) + (i == 0 ? 1 : 0)) * (kMaxG * (kD + 4));
+            return p.part + (2 * static_cast<size_t>(c_first + i) + (i == 0 ? 1 : 0)) * kSlot;
         };
         float M = -INFINITY, R = -INFINITY, ls = 0.f;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -327,6 +335,25 @@ __device__ __forceinline__ void merge_item(const WindowParams& p, long long c_fi
     }
 }
 
+// A chunk's partial into the sum of those before it, by log-sum-exp: a group's 128 threads,
+// thread gt column gt of every head.  (Every partial was written behind a barrier.)
+__device__ __noinline__ void add_chunk(float* sum, const float* part, int G, int gt, int grp) {
+    auto ex = [](float x, float ref) { return x == -INFINITY ? 1.f : pa_dev::ex2(x - ref); };   // (sums without a reference are 0 or NaN)
+    sync_group(grp);
+#pragma unroll 1
+    for (int g = 0; g < G; ++g) {
+        const float ra = sum[kMaxG * kD + g * 4 + 2], rb = part[kMaxG * kD + g * 4 + 2], r = fmaxf(ra, rb);
+        sum[g * kD + gt] = sum[g * kD + gt] * ex(ra, r) + part[g * kD + gt] * ex(rb, r);
+    }
+    sync_group(grp);                                               // the references are read
+    if (gt < G) {
+        float4* const at = reinterpret_cast<float4*>(sum + kMaxG * kD) + gt;
+        const float4 a = *at, b = reinterpret_cast<const float4*>(part + kMaxG * kD)[gt];
+        const float m = fmaxf(a.x, b.x);
+        *at = make_float4(m, a.y * ex(a.x, m) + b.y * ex(b.x, m), fmaxf(a.z, b.z), 0.f);
+    }
+}
+
 // One warp: the query rows of (s, h) into an N-side operand, and each head's score factor.
 template <bool CODE, bool WIDE, int GM>
 __device__ __forceinline__ void queries(const WindowParams& p, unsigned char* qt, float* qscale, int s, int h, int lane) {
@@ -367,7 +394,7 @@ __device__ __forceinline__ void queries(const WindowParams& p, unsigned char* qt
     }
 }
 
-template <bool CODE, bool WIDE, int GM>
+template <bool CODE, bool WIDE, int GM, bool CHUNKS>
 __global__ void __launch_bounds__(kThreads, 1)
 window_decode_kernel(const WindowParams p, int* counters, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap) {
@@ -475,6 +502,7 @@ window_decode_kernel(const WindowParams p, int* counters, const __grid_constant_
     pa_tc::fence_after_sync();
     const uint32_t tmem = m.tmem;
     const int G = p.G, Hkv = p.Hkv;
+    auto starts = [](int tile) { return (CHUNKS ? tile % kChunk : tile) == 0; };      // an item, or a chunk of one
     auto begin = [&](int q) {                                      // group q's first step
         Walk w;
         w.s = m.start_s[q];
@@ -515,16 +543,18 @@ window_decode_kernel(const WindowParams p, int* counters, const __grid_constant_
         };
         const int steps = n[grp];
         const long long range = blockIdx.x + grp * static_cast<long long>(gridDim.x), u0 = per * range;
-        // An item's result is written while the next one's first step is under way (its
-        // last value product is done by then)
-        struct Pending { int it, s, h, nt, begins, ends; long long u_first; } pend = {-1, 0, 0, 0, 0, 0, 0};
+        // An item's (or chunk's) result is written while the next one's first step is under
+        // way (its last value product is done by then).  cont, more: the range holds chunks
+        // of the item before, after this one
+        struct Pending { int it, s, h, nt, begins, ends, cont, more; long long u_first; } pend = {-1, 0, 0, 0, 0, 0, 0, 0, 0};
         auto finish = [&]() {
             const int ip = pend.it & 1;
             ok &= wait(&m.bars[kOFull0 + grp * 2 + ip], (pend.it >> 1) & 1, abort_flag);
             pa_tc::fence_after_sync();
             const size_t row0 = static_cast<size_t>(pend.s) * p.Hq + static_cast<size_t>(pend.h) * G;
-            const bool whole = pend.begins && pend.ends;
-            float* slot = p.part + (2 * static_cast<size_t>(range) + pend.begins) * (kMaxG * (kD + 4));
+            const bool whole = pend.begins && pend.ends && !(CHUNKS && pend.cont);
+            float* const sum = p.part + (2 * static_cast<size_t>(range) + pend.begins) * kSlot;
+            float* const slot = CHUNKS && pend.cont ? p.part + (4 * static_cast<size_t>(gridDim.x) + range) * kSlot : sum;
             const uint32_t od = tmem + C::kOCol + (grp * 2 + ip) * C::kNP + lane_sel;
 #pragma unroll 1
             for (int g0 = 0; g0 < GM; g0 += 4) {                   // four heads at a time: their columns of every part
@@ -559,7 +589,8 @@ window_decode_kernel(const WindowParams p, int* counters, const __grid_constant_
             pa_tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) arrive(&m.bars[kOEmpty0 + grp * 2 + ip]);
-            if (!whole) {
+            if (CHUNKS && pend.cont) add_chunk(sum, slot, G, gt, grp);
+            if (!whole && !(CHUNKS && pend.more)) {
                 // the last of the item's groups to get here merges them, in their order
                 const long long c_first = pend.u_first / per, c_last = (pend.u_first + pend.nt - 1) / per;
                 const int item = pend.s * Hkv + pend.h, parts = static_cast<int>(c_last - c_first) + 1;
@@ -575,14 +606,16 @@ window_decode_kernel(const WindowParams p, int* counters, const __grid_constant_
             }
         };
         long long u_first = u0;                                    // the item's first step in the list
-        int it = -1;                                               // items begun
+        int it = -1, cont = 0;                                     // items (chunks) begun
         uint32_t v_ph = 0;                                         // bit st: parity of slot st's next phase
         Walk w = {};
         if (steps > 0) w = begin(grp);
         for (int j = 0; j < steps; ++j) {
-            const bool first = j == 0 || w.tile == 0, last = j == steps - 1 || w.tile == w.nt - 1;
+            const bool first = j == 0 || starts(w.tile);
+            const bool last = j == steps - 1 || w.tile == w.nt - 1 || (CHUNKS && (w.tile + 1) % kChunk == 0);
             if (first) {
                 ++it;
+                if constexpr (CHUNKS) cont = j > 0 && w.tile > 0;
                 u_first = u0 + j - w.tile;
             }
             const int par = j & 1;
@@ -853,7 +886,7 @@ window_decode_kernel(const WindowParams p, int* counters, const __grid_constant_
                     next_four(r_o);
                     next_four(l);
                 }
-                pend = {it, w.s, w.h, w.nt, u_first >= u0, w.tile == w.nt - 1, u_first};
+                pend = {it, w.s, w.h, w.nt, u_first >= u0, w.tile == w.nt - 1, cont, CHUNKS && j < steps - 1 && w.tile < w.nt - 1, u_first};
             }
             w.next(p);
         }
@@ -880,7 +913,7 @@ window_decode_kernel(const WindowParams p, int* counters, const __grid_constant_
             if (lane < kStepBlks && b < v.nv) e.x = __ldg(p.tables + static_cast<size_t>(v.s) * p.max_blocks + v.block(b));
             e.s = v.s;
             e.h = v.h;
-            e.first = v.tile == 0;
+            e.first = starts(v.tile);
             v.next(p);
             if (q) w[1] = v;
             else w[0] = v;
@@ -1013,7 +1046,8 @@ window_decode_kernel(const WindowParams p, int* counters, const __grid_constant_
         int blocks_prev = 0;
         for (int j = 0; j < steps; ++j) {
             const int pl = place(grp, j), st = pl % C::kStages, sb = grp * 2 + (j & 1);
-            const bool first = j == 0 || w.tile == 0, last = j == steps - 1 || w.tile == w.nt - 1;
+            const bool first = j == 0 || starts(w.tile);
+            const bool last = j == steps - 1 || w.tile == w.nt - 1 || (CHUNKS && (w.tile + 1) % kChunk == 0);
             if (first) {
                 ++it;
                 if (!wait(&m.bars[kQFull0 + grp * 2 + (it & 1)], (it >> 1) & 1, abort_flag)) { ok = false; break; }
@@ -1065,10 +1099,10 @@ window_decode_kernel(const WindowParams p, int* counters, const __grid_constant_
     if (warp == 9) pa_tc::tmem_free<C::kTmemCols>(tmem);
 }
 
-template <bool CODE, bool WIDE, int GM>
+template <bool CODE, bool WIDE, int GM, bool CHUNKS = false>
 int launch(pa_pool* pool, const WindowParams& p, int* counters, cudaStream_t st) {
     using C = Cfg<CODE, WIDE, GM>;
-    auto kernel = window_decode_kernel<CODE, WIDE, GM>;
+    auto kernel = window_decode_kernel<CODE, WIDE, GM, CHUNKS>;
     static std::atomic<uint64_t> done{0};
     if (!pa_detail::allow_smem(kernel, pool->device, C::kSmem, done)) return PA_ERR_CUDA;
     const cudaError_t e = pa_detail::launch_pdl(kernel, dim3(pool->num_sms), dim3(kThreads), C::kSmem, st, p, counters,
@@ -1090,21 +1124,28 @@ bool window_decode_tc_eligible(const pa_pool* pool, const WindowParams& p) {
            tiles * (pool->dtype == PA_BF16 ? kD : kBlk) < (1LL << 31);
 }
 
-// Bytes of the counters (one per item) and of the partials (two per range, two ranges per CTA).
+// Bytes of the counters (one per item) and of the partials (two per range and one for a
+// chunk, two ranges per CTA).
 size_t window_decode_tc_counters(const pa_pool* pool, int S) {
     return (static_cast<size_t>(S) * pool->kv_heads * sizeof(int) + 255) / 256 * 256;
 }
 size_t window_decode_tc_partials(const pa_pool* pool) {
-    return static_cast<size_t>(pool->num_sms) * 4 * kMaxG * (kD + 4) * sizeof(float);
+    return static_cast<size_t>(pool->num_sms) * 6 * kSlot * sizeof(float);
 }
 
 int launch_window_decode_tc(pa_pool* pool, const WindowParams& p, int* counters, cudaStream_t st) {
     const int rc = ensure_tensor_maps(pool);
     if (rc != PA_OK) return rc;
     const bool code = is_code(pool->dtype), wide = !p.out_bf16;
+    // whether an item's steps in one range can be more than a chunk: by the table's width and
+    // the window, which the host knows
+    const int64_t blocks = std::min<int64_t>(p.max_blocks, (static_cast<int64_t>(p.window) + p.sinks) / kBlk + 3);
+    const int64_t steps = (blocks + kStepBlks - 1) / kStepBlks, ranges = 2 * pool->num_sms;
+    const bool chunks = code && wide && std::min(steps, (steps * p.S * p.Hkv + ranges - 1) / ranges) > kChunk;
     auto pick = [&](auto gm) {
         constexpr int GM = decltype(gm)::value;
-        return code ? (wide ? launch<true, true, GM>(pool, p, counters, st) : launch<true, false, GM>(pool, p, counters, st))
+        return chunks ? launch<true, true, GM, true>(pool, p, counters, st)
+             : code ? (wide ? launch<true, true, GM>(pool, p, counters, st) : launch<true, false, GM>(pool, p, counters, st))
                     : (wide ? launch<false, true, GM>(pool, p, counters, st) : launch<false, false, GM>(pool, p, counters, st));
     };
     if (p.G <= 4) return pick(std::integral_constant<int, 4>{});
