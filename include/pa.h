@@ -13,7 +13,9 @@
  *     launched.  Errors only the GPU can see (a block id or slot outside the
  *     pool) make the kernel skip the offending access and record the first
  *     such code in the pool's device error word; pa_get_error reports it.
- *     No call traps or aborts.
+ *     No call traps or aborts.  A kernel that records PA_ERR_CUDA gave up a
+ *     wait inside the GPU: its outputs, and those of later calls that use the
+ *     pool's workspaces, are not defined; destroy the pool.
  *   - Device pointers: every tensor argument marked "device" is GPU memory
  *     owned by the caller, on the device the pool was created on, and aligned
  *     to its elements (the attention calls' q to 16 bytes; else
@@ -21,10 +23,11 @@
  *   - Streams: `stream` is a cudaStream_t passed as void*.  NULL means the
  *     legacy default stream.  Every GPU call is asynchronous on it.
  *   - CUDA graphs: once the pool's workspace holds the batch (a first call of
- *     the same shape, or pa_decode_reserve), pa_append_kv, pa_copy_blocks,
- *     pa_decode, pa_append_decode, pa_decode_noalloc and pa_prefill only
- *     launch kernels on `stream`, so they may be captured into a graph and
- *     replayed.  pa_decode_shared uploads its group description with a
+ *     the same shape, or pa_decode_reserve, pa_decode_window_reserve),
+ *     pa_append_kv, pa_append_rope, pa_read_kv, pa_copy_blocks, pa_decode,
+ *     pa_decode_window, pa_append_decode, pa_decode_noalloc, pa_prefill and
+ *     pa_prefill_window only launch kernels on `stream`, so they may be
+ *     captured into a graph and replayed.  pa_decode_shared uploads its group description with a
  *     pageable copy when the description changes, pa_get_error synchronises:
  *     keep those two out of a capture.
  *
@@ -301,8 +304,9 @@ int pa_decode(pa_pool *pool, const void *q, int num_seqs, int num_q_heads,
  * tensor-core path (bf16 pools, and fp8 pools whose codes the kernel widens)
  * the write is done inside the decode kernel by the warp that reads that block
  * (one launch fewer per step; an fp8 pool's codes are quantized there exactly
- * as pa_append_kv quantizes them); other shapes run pa_append_kv and pa_decode
- * back to back.  Copy-on-write copies, if any, must be issued before
+ * as pa_append_kv quantizes them); other shapes, and PA_FP8E4M3_BLOCK pools, run
+ * pa_append_kv and pa_decode back to back, and there a slot is not compared with
+ * context_lens: the token is written where the slot says.  Copy-on-write copies, if any, must be issued before
  * (pa_copy_blocks). */
 int pa_append_decode(pa_pool *pool, const void *k, const void *v, const int64_t *slot_mapping,
                      const void *q, int num_seqs, int num_q_heads, const int32_t *block_tables,
@@ -319,7 +323,8 @@ int pa_decode_reserve(pa_pool *pool, int max_seqs, int max_q_heads);
  * window >= 1, sinks >= 0 (else PA_ERR_INVALID_ARG); a window no shorter than
  * every context is plain attention.  A context length of 0 gives a zero row.
  * Table entries of blocks that hold no visible key are never read, so a caller
- * may free those blocks and leave -1 there.
+ * that keeps its own tables may free those blocks and leave -1 there (the block
+ * manager below frees whole requests).
  * Every pool type, block size and head width; num_q_heads / kv_heads <= 16,
  * S <= 16384.  On a PA_FP8E4M3_BLOCK pool pa_decode, pa_append_decode (append,
  * then decode), pa_decode_shared (every sequence on its own) and pa_prefill run
@@ -372,7 +377,7 @@ int pa_decode_window_reserve(pa_pool *pool, int max_seqs, int max_q_heads);
  * selects); each member's private suffix goes through the ordinary split
  * path, and the partials are merged by log-sum-exp.  Groups with fewer than two members
  * or no shared block are ignored; shapes outside the bf16 tensor-core path
- * (see pa_decode) fall back to pa_decode.  The device checks that members'
+ * (see pa_decode), PA_FP8E4M3_BLOCK pools among them, fall back to pa_decode.  The device checks that members'
  * leading entries agree and that their contexts cover the shared span, and
  * records PA_ERR_INVALID_ARG otherwise (the result is then undefined).
  * The description is uploaded to the device when it differs from the

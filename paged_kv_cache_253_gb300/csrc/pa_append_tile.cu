@@ -16,15 +16,17 @@
 // block by a kernel in front (pa_kv_scaled.cu).
 //
 // Measured (8 KV heads, block-scaled): 64 tokens of 64 sequences appended and read back
-// 17 us, both calls' launches; 4779 tokens 27 us, of which notes 4, tiles 14, read-back 9;
-// four images' 9892 tokens with 32 query heads rotated 80 us (notes 4, queries 27 at 6.0
-// TB/s, tiles 35, read-back 12).  The tiles are bound by their instructions, 700 to 1200
+// 16 us, both calls' launches (the kernels alone, one by one: 6 and 5); 5378 tokens 27 us
+// (notes 3, tiles 18, read-back 10); four images' 9896 tokens with 32 query heads rotated
+// 80 us (notes 3, queries 29 at 5.6 TB/s, tiles 37, read-back 13).  The tiles are bound by their instructions, 700 to 1200
 // for a lane's 64 elements, and by four dependent loads in a row before them.
 //
 // Angles: positions times frequencies in turns, as 64-bit fixed-point fractions
 // of a turn, where the multiplication wraps as angles do.  Frequencies are
 // converted once per CTA in 64-bit floating point, whose rate on this GPU is 2
-// operations per cycle and SM.  Positions up to 2^31 keep 2^-33 of a turn.
+// operations per cycle and SM.  A frequency below 1 is off by up to 2^-55.6 of a turn, its
+// product with 1 / 2 pi being rounded to 53 bits, so an angle by that times the position:
+// 2^-35.6 of a turn at 2^20, 2^-24.6 at 2^31.
 #include <algorithm>
 #include <cstdint>
 
@@ -211,7 +213,7 @@ struct TileParams {
 
 // A CTA takes `per` tokens of the list: one while it searches the slots itself, else
 // 16, of which about one leads a block; gridDim.y CTAs share their rows and tiles.  (A CTA per token, 15 of 16 with nothing to store, spent 34 us on a
-// prefill step's 4779 tokens, most of it starting CTAs.)
+// prefill step's 5378 tokens, most of it starting CTAs.)
 template <int KIND, bool ROPE>
 __global__ void __launch_bounds__(kThreads, ROPE ? 2 : 3) append_tile_kernel(const TileParams p, const RopeParams r, int per) {
     __shared__ __align__(16) float s_cs[kB][kD];                                   // of a block's new tokens: cosines, sines
@@ -668,8 +670,10 @@ int launch_append_tile(pa_pool* p, const void* k, const void* v, const int64_t* 
             r.q = nullptr;
         }
     }
-    // few tokens: a warp per (KV head, keys or values).  Many: two per warp, so that a
-    // prefill step's CTAs run in one wave (a note's upper half has room for 32 CTAs)
+    // few tokens: a warp per (KV head, keys or values).  Many, rotated: two per warp, which
+    // forms a block's angles half as often (9896 tokens: 619 CTAs, two waves of the 304 that
+    // fit and eleven CTAs more; 5378 without rotation: 674, one and a half waves of 456).  A
+    // note's upper half has room for 32 CTAs
     const int per = T > kDirect ? kB : 1, items = T > kDirect && rope.half > 0 ? 2 : 1;
     const dim3 grid((T + per - 1) / per, std::min(32, (2 * p->kv_heads + kWarps * items - 1) / (kWarps * items)));
     // (bf16 pools and pools with one scale come here for pa_append_rope alone)

@@ -46,8 +46,8 @@
 // wait is bounded (see pa_window_tc.cu).
 //
 // Measured (32 query, 8 KV heads): 8 sequences of 32768 .. 131072 tokens,
-// block-scaled, 198 us, 5.9 TB/s; 64 of 128 .. 2048, 47 us, 3.0 TB/s; 64 on a window of
-// 1024, bf16, 55 us, 4.9 TB/s; 256 on a window of 512, 64 query heads, fp32 out, 138 us,
+// block-scaled, 195 us, 6.0 TB/s; 64 of 128 .. 2048, 47 us, 3.0 TB/s; 64 on a window of
+// 1024, bf16, 55 us, 4.9 TB/s; 256 on a window of 512, 64 query heads, fp32 out, 143 us,
 // 2.0 TB/s.  Long ranges run at the memory's rate; where items are a few steps long
 // the weights' chain of waits (about 4500 cycles a step, two under way) and the ends of
 // items set the pace.  Three groups, a warp that plans the copies for the others and

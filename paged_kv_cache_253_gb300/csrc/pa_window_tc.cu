@@ -36,11 +36,11 @@
 // tile's threads compute weights; four MMA-sized TMEM buffers (two S/P, two O)
 // fill TMEM, and two K and two V stages beside both Q tiles fill 192 KB.
 //
-// Measured (32 query, 8 KV heads): a prompt of 8191 tokens, window 2048, bf16, 225 us,
-// 1.07 PFLOP/s of the visible scores' and values' products, 0.57 of the matrix rate
+// Measured (32 query, 8 KV heads): a prompt of 8191 tokens, window 2048, bf16, 221 us,
+// 1.09 PFLOP/s of the visible scores' and values' products, 0.59 of the matrix rate
 // (steps also compute what their masks hide, 6 % more); 16 chunks on up to 4096
-// cached tokens, block-scaled, 210 us, 0.87 PFLOP/s.  A step of two tiles takes 3100
-// (bf16) to 3700 (codes) cycles, of which the MMAs need 2600; a CTA spends another
+// cached tokens, block-scaled, 216 us, 0.84 PFLOP/s.  A step of two tiles takes about 3000
+// (bf16) to 3800 (codes) cycles, of which the MMAs need 2600; a CTA spends another
 // 14000 or so, a third of a 10-step one, on its queries, its first keys, its results
 // and the change to the next CTA.  A form whose CTAs stay and take tiles by ticket
 // was a tenth to a quarter slower (its softmax warps spilled), and code for queries and results
