@@ -215,8 +215,8 @@ int pa_append_kv(pa_pool *pool, const void *k, const void *v, const int64_t *slo
  * scratch between calls, like PA_FP8E4M3_BLOCK pools: two such calls, or one and
  * a pa_append_kv to a block-scaled pool, must not overlap on the GPU.  bf16 and
  * PA_FP8E4M3 pools of 16-token blocks of 128-wide heads allocate that scratch (72
- * bytes per block) with their first call of more than 512 tokens; where that is not
- * possible (a first call inside a capture, no memory) a slower kernel runs. */
+ * bytes per block) with their first call of more than 512 tokens, inside a capture
+ * too; without memory for it a slower kernel runs. */
 int pa_append_rope(pa_pool *pool, const void *q, int64_t q_stride, int num_q_heads,
                    const void *k, int64_t k_stride, const void *v, int64_t v_stride,
                    const int64_t *slot_mapping, int num_tokens, const int32_t *positions,

@@ -616,30 +616,32 @@ bool append_tile_eligible(const pa_pool* p, const void* k, const void* v, const 
            (!r.q || (aligned16(r.q) && aligned16(r.q_out) && r.q_stride % 8 == 0));
 }
 
-// False where it cannot be made: under a capture (no allocation there), or without memory
-// for it.  The plain kernels need none.
-bool append_notes_ready(pa_pool* p, int T, cudaStream_t st) {
+// False without memory for it; the plain kernels need none.  A first call inside a capture
+// makes it too: allocated and cleared beside the capture, on a stream of its own, which a
+// thread in relaxed mode may do.
+bool append_notes_ready(pa_pool* p, int T) {
     if (T <= kDirect || p->app_mask) return true;
-    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(st, &capture) != cudaSuccess || capture != cudaStreamCaptureStatusNone) {
-        cudaGetLastError();
-        return false;
-    }
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return false;
     const size_t nb = static_cast<size_t>(p->num_blocks);
     void *mask = nullptr, *token = nullptr;
-    // (the clearing is not ordered with the caller's stream: waited for)
-    if (cudaMalloc(&mask, nb * sizeof(unsigned long long)) != cudaSuccess ||
-        cudaMalloc(&token, nb * kB * sizeof(int32_t)) != cudaSuccess ||
-        cudaMemset(mask, 0, nb * sizeof(unsigned long long)) != cudaSuccess ||
-        cudaStreamSynchronize(cudaStreamLegacy) != cudaSuccess) {
+    cudaStream_t own = nullptr;
+    const bool ok = cudaMalloc(&mask, nb * sizeof(unsigned long long)) == cudaSuccess &&
+                    cudaMalloc(&token, nb * kB * sizeof(int32_t)) == cudaSuccess &&
+                    cudaStreamCreateWithFlags(&own, cudaStreamNonBlocking) == cudaSuccess &&
+                    cudaMemsetAsync(mask, 0, nb * sizeof(unsigned long long), own) == cudaSuccess &&
+                    cudaStreamSynchronize(own) == cudaSuccess;
+    if (own) cudaStreamDestroy(own);
+    if (!ok) {
         cudaGetLastError();
         cudaFree(mask);
         cudaFree(token);
-        return false;
+    } else {
+        p->app_mask = static_cast<unsigned long long*>(mask);
+        p->app_token = static_cast<int32_t*>(token);
     }
-    p->app_mask = static_cast<unsigned long long*>(mask);
-    p->app_token = static_cast<int32_t*>(token);
-    return true;
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    return ok;
 }
 
 int launch_append_tile(pa_pool* p, const void* k, const void* v, const int64_t* slots, int T, const RopeParams& rope,

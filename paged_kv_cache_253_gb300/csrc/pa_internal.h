@@ -252,7 +252,7 @@ int launch_append_notes(pa_pool* p, const int64_t* slots, int T, cudaStream_t st
 // Appends by whole block tiles (16-token blocks, head width 128), every pool type
 // but f32, and the read-back of such pools (pa_append_tile.cu).
 bool append_tile_eligible(const pa_pool* p, const void* k, const void* v, const RopeParams& r);
-bool append_notes_ready(pa_pool* p, int T, cudaStream_t st);     // its scratch for T tokens is there (made if need be)
+bool append_notes_ready(pa_pool* p, int T);     // its scratch for T tokens is there (made if need be)
 int launch_append_tile(pa_pool* p, const void* k, const void* v, const int64_t* slots, int T,
                        const RopeParams& rope, cudaStream_t st);
 bool read_tile_eligible(const pa_pool* p, const void* k, const void* v);

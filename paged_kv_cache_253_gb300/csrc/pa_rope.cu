@@ -115,7 +115,7 @@ extern "C" int pa_append_rope(pa_pool* pool, const void* q, int64_t q_stride, in
     r.interleaved = interleaved != 0;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (pool->scales) return pa_detail::launch_append_scaled(pool, k, v, slot_mapping, num_tokens, r, st);
-    if (pa_detail::append_tile_eligible(pool, k, v, r) && pa_detail::append_notes_ready(pool, num_tokens, st))
+    if (pa_detail::append_tile_eligible(pool, k, v, r) && pa_detail::append_notes_ready(pool, num_tokens))
         return pa_detail::launch_append_tile(pool, k, v, slot_mapping, num_tokens, r, st);
     const int64_t num_slots = static_cast<int64_t>(pool->num_blocks) * pool->block_size;
     auto launch = [&](auto* kp, auto* vp, auto kernel) {

@@ -153,3 +153,27 @@ def test_pointers_that_are_not_aligned_to_their_elements_are_refused(kind):
             assert L.pa_prefill(pool.handle, a, 1, 8, a, 1, 1, t, 1, n, 0.1, o, dt, None) == L.PA_ERR_INVALID_ARG
     assert L.pa_prefill_window(pool.handle, a, 1, 8, a + 2, 1, 1, a, 1, a, 9, 0, 0.1, a, L.PA_F32, None) == L.PA_ERR_INVALID_ARG
     assert pool.get_error() == 0 and not pool.export()[0].any()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+def test_a_first_call_inside_a_capture_is_the_call(kind):
+    """The scratch of a long rotary append is made beside the capture: replays run the kernels that
+    an ordinary call runs, bit for bit, and an ordinary call may come before the first replay."""
+    g = torch.Generator().manual_seed(6)
+    T, H, Hq, D = 5000, 2, 4, 128
+    q, k, v = (torch.randn(T, h, D, generator=g).bfloat16().to(DEV) for h in (Hq, H, H))
+    slots = torch.randperm(400 * 16, generator=g)[:T].to(DEV)
+    pos = torch.randint(0, 1 << 20, (T,), generator=g, dtype=torch.int32).to(DEV)
+    inv = (1e6 ** (-torch.arange(64, dtype=torch.float64) / 64)).float().to(DEV)
+    plain, pool = KVPool(400, 16, H, D, kind, DEV), KVPool(400, 16, H, D, kind, DEV)
+    want = plain.append_rope(q, k, v, slots, pos, inv), *plain.export()
+    out = torch.zeros_like(q)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pool.append_rope(q, k, v, slots, pos, inv, q_out=out)
+    for call in (lambda: pool.append_rope(q, k, v, slots, pos, inv, q_out=out), graph.replay, graph.replay):
+        out.zero_()
+        pool.import_(*(torch.zeros_like(x) for x in pool.export()))
+        call()
+        assert all(torch.equal(a, b) for a, b in zip(want, (out, *pool.export())))
+    assert pool.get_error() == 0
